@@ -2,14 +2,18 @@
 // that a plan (include/qroute.h) gives to each weight set e, on packed Q4_K,
 // NVFP4 and TQ1_0 matrices.
 //
-// Two kernels, chosen by the number of rows and tiles (launch_routed):
+// Kernels, chosen by the number of rows and tiles (launch_routed):
 //  - few rows (decode), or too few tiles for the CUs: every wave streams its own
 //    weight rows through LDS and decodes them straight into matrix-core operands,
 //    once per 16 rows (routed_rows_kernel);
-//  - many rows (prefill): the matrix cores bound it, so the weights are decoded
-//    once per tile of tokens into LDS, with the prefill's loop
-//    (routed_tile_kernel).
+//  - many rows (prefill) of NVFP4 and TQ1_0, whose weights are exact in 16 bits:
+//    decoded once per tile of tokens into LDS, with the prefill's loop
+//    (routed_tile_kernel);
+//  - many rows of Q4_K, whose weights are not (a 16-bit weight is off by up to 2^-11
+//    of itself): the first kernel's arithmetic with 64 tokens a workgroup
+//    (routed_q4k_kernel).
 #include <algorithm>
+#include <type_traits>
 
 #include "device.hpp"
 #include "epilogue.hpp"
@@ -155,7 +159,14 @@ struct Q4kRows {
   // (high); times scale * 2^10 or scale * 2^6 it is scale * q * 2^-14, at most
   // 945 * 2^-14 and a multiple of 2^-14: exact, and a normal number for the
   // matrix cores.
-  static __device__ __forceinline__ void mma(const Raw& raw, const X& x, int g, f32x4& acc) {
+  // What a unit of one weight row is scaled by: both groups' scales as fp16 pairs, the
+  // mins as the K slots of split_sums, and d * 2^14 and dmin of the block.
+  struct Scales {
+    f16x2 a0, a1;
+    u32x4 mins;
+    float d, dmin;
+  };
+  static __device__ __forceinline__ Scales scales(const Raw& raw, int g) {
     // 6-bit scales and mins of groups 2 g and 2 g + 1, as bytes 0 and 1
     const bool hi = g >= 2;
     const unsigned sh = 16u * (unsigned)(g & 1), shm = hi ? sh + 4u : sh;
@@ -165,26 +176,37 @@ struct Q4kRows {
     const unsigned mn = ((na >> shm) & ma) | ((raw.hdr.z >> (sh + 2u)) & mb);
     // both scales as fp16: 1024 + scale under the exponent of 1024, minus 1024
     const f16x2 s2 = (as_h2(__builtin_amdgcn_perm(0x64646464u, sc, 0x04010400u)) + f16x2{-1024, -1024}) * f16x2{1024, 64};
-    const f16x2 a0 = {s2.x, s2.x}, a1 = {s2.y, s2.y};
-    const unsigned v[8] = {raw.q0.x, raw.q0.y, raw.q0.z, raw.q0.w, raw.q1.x, raw.q1.y, raw.q1.z, raw.q1.w};
-    f32x4 q = {0.f, 0.f, 0.f, 0.f};
-    const auto low = [&](unsigned b) { return __builtin_bit_cast(unsigned, as_h2(b & 0x000F000Fu) * a0); };
-    const auto high = [&](unsigned b) { return __builtin_bit_cast(unsigned, as_h2(b & 0x00F000F0u) * a1); };
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const unsigned b0 = v[2 * s], b1 = v[2 * s + 1];
-      q = mfma16(x.f[s], u32x4{low(b0), low(b0 >> 8), low(b1), low(b1 >> 8)}, q);
-      q = mfma16(x.f[4 + s], u32x4{high(b0), high(b0 >> 8), high(b1), high(b1 >> 8)}, q);
-    }
     // mins as bf16: the upper halves of the (exact) fp32 values
     const unsigned m0 = __builtin_bit_cast(unsigned, (float)(mn & 0xFFu));
     const unsigned m1 = __builtin_bit_cast(unsigned, (float)((mn >> 8) & 0xFFu));
-    const u32x4 mf = {__builtin_amdgcn_perm(m0, m0, 0x07060302u), __builtin_amdgcn_perm(m1, m0, 0x07060302u),
-                      __builtin_amdgcn_perm(m1, m1, 0x07060302u), 0u};
-    const f32x4 least = mfma16_bf(x.sums, mf, f32x4{0.f, 0.f, 0.f, 0.f});
-    const float d = f16lo(raw.hdr.x) * 16384.f, dmin = f16hi(raw.hdr.x);
+    return Scales{f16x2{s2.x, s2.x}, f16x2{s2.y, s2.y},
+                  u32x4{__builtin_amdgcn_perm(m0, m0, 0x07060302u), __builtin_amdgcn_perm(m1, m0, 0x07060302u),
+                        __builtin_amdgcn_perm(m1, m1, 0x07060302u), 0u},
+                  f16lo(raw.hdr.x) * 16384.f, f16hi(raw.hdr.x)};
+  }
+  // B operands of qs bytes 8 s .. + 8 of the lane's 32: low nibbles (x operand s)
+  // and high ones (operand 4 + s)
+  static __device__ __forceinline__ void weights(const Raw& raw, const Scales& sc, int s, u32x4& lo, u32x4& hi) {
+    const u32x4 v = s < 2 ? raw.q0 : raw.q1;
+    const unsigned b0 = s % 2 ? v.z : v.x, b1 = s % 2 ? v.w : v.y;
+    const auto low = [&](unsigned b) { return __builtin_bit_cast(unsigned, as_h2(b & 0x000F000Fu) * sc.a0); };
+    const auto high = [&](unsigned b) { return __builtin_bit_cast(unsigned, as_h2(b & 0x00F000F0u) * sc.a1); };
+    lo = u32x4{low(b0), low(b0 >> 8), low(b1), low(b1 >> 8)};
+    hi = u32x4{high(b0), high(b0 >> 8), high(b1), high(b1 >> 8)};
+  }
+  static __device__ __forceinline__ void mma(const Raw& raw, const X& x, int g, f32x4& acc) {
+    const Scales sc = scales(raw, g);
+    f32x4 q = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(d, q[i], __builtin_fmaf(-dmin, least[i], acc[i]));
+    for (int s = 0; s < 4; ++s) {
+      u32x4 lo, hi;
+      weights(raw, sc, s, lo, hi);
+      q = mfma16(x.f[s], lo, q);
+      q = mfma16(x.f[4 + s], hi, q);
+    }
+    const f32x4 least = mfma16_bf(x.sums, sc.mins, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(sc.d, q[i], __builtin_fmaf(-sc.dmin, least[i], acc[i]));
   }
 
   // Staged: a unit's 144-byte blocks of 16 rows, row after row, so that a
@@ -217,11 +239,15 @@ struct Q4kRows {
   }
   // 16-byte granule j of a unit of one token (elements 8 j .. + 8), for the wave's
   // 64 threads' (token, j): lane t holds j = t % 32
-  static __device__ __forceinline__ void store_x(unsigned char* xs, int token, int j, u32x4 v) {
+  // their sum over the granule's group of 32, in all four lanes that hold it
+  static __device__ __forceinline__ float group_sum(u32x4 v) {
     float s = dot2h(v.x, 0x3C003C00u, dot2h(v.y, 0x3C003C00u, dot2h(v.z, 0x3C003C00u, dot2h(v.w, 0x3C003C00u, 0.f))));
     s += dpp_xor1(s);
-    s += dpp_xor2(s);  // a group of 32: four neighbouring granules
-    const float t = shfl_xor(s, 4);
+    s += dpp_xor2(s);
+    return s;
+  }
+  static __device__ __forceinline__ void store_x(unsigned char* xs, int token, int j, u32x4 v) {
+    const float s = group_sum(v), t = shfl_xor(s, 4);
     *reinterpret_cast<u32x4*>(xs + x_frag(j & 7, j >> 3, token)) = even_odd(v);
     if ((j & 7) == 0) *reinterpret_cast<u32x4*>(xs + x_frag(8, j >> 3, token)) = split_sums(s, t);
   }
@@ -544,6 +570,167 @@ __global__ __launch_bounds__(64 * RW * KW, RW * KW == 4 ? 3 : 2) void routed_row
       store_y(a.y, a.y_dtype, (int64_t)(t.first + 4 * g + i) * a.m + n0 + col, acc[i]);
 }
 
+// ---- many rows, Q4_K -----------------------------------------------------------------
+//
+// The arithmetic of Q4kRows with 64 tokens a workgroup, so that weights are decoded once
+// for 64 rows: a wave takes 32 weight rows and multiplies them with every 16
+// tokens' operands, which the workgroup's 8 waves read from LDS.  No weight is rounded:
+// scale * q is exact in fp16, and the sums of a block are scaled by its d and its mins
+// subtracted in fp32.
+//
+// While a unit is multiplied, its successor's packed bytes are copied to LDS and read
+// into registers at the unit's end; the activations go from registers, loaded a unit
+// ahead, into operand order in the other of two LDS buffers.  One barrier a unit.
+//
+// Q4_K, 2048 tokens x 2 over 8 sets of 14336 x 4096: 725 us (0.66 PFLOP/s of the weights'
+// own products), bound by issue: 370 VALU instructions (decoding 200, activations and
+// their sums 75, scaling 64) and 72 MFMAs a unit and wave.  With weights rounded to fp16
+// in LDS and tiles of 256 x 256 the same took 615 us, but 64 to 512 rows of each of the
+// sets took 115 to 160 us, 82 to 140 like this.  Tiles of 96 tokens: 719 us, but 128 us
+// against 101 for 512 rows of one set; 48 weight rows a wave: 728, 133; 16 waves of 16
+// rows: 788, 104.
+constexpr int kQ4kBT = 64;   // tokens of a workgroup
+constexpr int kQ4kBN = 256;  // its weight rows
+constexpr int kQ4kWaves = 8;
+
+__global__ __launch_bounds__(64 * kQ4kWaves, 2) void routed_q4k_kernel(RoutedArgs a) {
+  typedef Q4kRows F;
+  constexpr int BT = kQ4kBT, TT = BT / 16, RW = kQ4kWaves, NR = kQ4kBN / (16 * RW);
+  constexpr int XG = 8 * TT / RW;  // granules of a unit per thread
+  static_assert(XG == 4, "a quad's four lanes hold the sums of a thread's four tokens");
+  constexpr int kStage = NR * F::kStage, kChunks = NR * 144, kCopies = (kChunks + 63) / 64;
+  __shared__ __attribute__((aligned(256))) unsigned char ws[RW * kStage];
+  __shared__ __attribute__((aligned(256))) unsigned char xs[2 * TT * F::kXBytes];
+  const int tile = (int)(blockIdx.x / (unsigned)a.groups), group = (int)blockIdx.x - tile * a.groups;
+  const RoutedTile t = find_tile(a.offsets, a.e_count, a.n, BT, tile);
+  if (t.rows == 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, g = lane >> 4;
+  const int n0 = (group * RW + wave) * 16 * NR;
+  const int units = a.k / 256;
+  const auto wd = F::desc(a.w + t.e * a.expert_bytes, a.m, a.k, n0, max(0, min(16 * NR, a.m - n0)));
+  uint32_t wo[kCopies];
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) {
+    const int c = 64 * i + lane, r = c / 9;
+    wo[i] = (uint32_t)r * (uint32_t)(a.k / 256 * 144) + 16u * (uint32_t)(c % 9);
+  }
+  unsigned char* const mine = ws + wave * kStage;
+  const auto copy_w = [&](int u) {
+    copy_chunks<kChunks>(wd.r, mine, wo, 144u * (uint32_t)u, u < units);
+    compiler_fence();
+  };
+  const auto xr = x_rsrc(a, t);
+  const int token = 2 * wave + (lane >> 5), j = lane & 31;  // of 2 RW tokens a round
+  uint32_t xo[XG];
+#pragma unroll
+  for (int h = 0; h < XG; ++h) xo[h] = x_offset(a, t, 2 * RW * h + token) + 16u * (uint32_t)j;
+  u32x4 xq[XG];
+  const auto load_x = [&](int u, int h) { xq[h] = ld128s(xr, xo[h], u < units ? 512u * (uint32_t)u : kDeadUnit); };
+  float sum;  // of the group that lane j % 4 = h of each four holds for token h
+  const auto store_x = [&](int u, int h) {
+    const int i = 2 * RW * h + token;
+    const float v = F::group_sum(xq[h]);
+    *reinterpret_cast<u32x4*>(xs + ((u & 1) * TT + (i >> 4)) * F::kXBytes + x_frag(j & 7, j >> 3, i & 15)) = even_odd(xq[h]);
+    sum = h == 0 || (j & 3) == h ? v : sum;
+  };
+  const auto store_sums = [&](int u) {  // (both halves of eight lanes write the same)
+    const int i = 2 * RW * (j & 3) + token;
+    const float other = shfl_xor(sum, 4);
+    *reinterpret_cast<u32x4*>(xs + ((u & 1) * TT + (i >> 4)) * F::kXBytes + x_frag(8, j >> 3, i & 15)) =
+        F::split_sums(j & 4 ? other : sum, j & 4 ? sum : other);
+  };
+  typename F::Raw raw[NR];
+  const auto read_w = [&]() {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) raw[r] = F::read(wd, mine, 0, 16 * r + col, g, 0, a.k);
+  };
+  f32x4 acc[TT][NR];
+#pragma unroll
+  for (int i = 0; i < TT; ++i)
+#pragma unroll
+    for (int r = 0; r < NR; ++r) acc[i][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  copy_w(0);
+#pragma unroll
+  for (int h = 0; h < XG; ++h) load_x(0, h);
+#pragma unroll
+  for (int h = 0; h < XG; ++h) {
+    store_x(0, h);
+    load_x(1, h);
+  }
+  store_sums(0);
+  wait_vm<XG>();
+  read_w();
+  lds_barrier();
+  const auto run = [&](auto nc) {
+    constexpr int NT = decltype(nc)::value;
+    for (int u = 0; u < units; ++u) {
+      // the packed bytes of this unit are in registers
+      copy_w(u + 1);
+      const unsigned char* const xu = xs + (u & 1) * TT * F::kXBytes;
+      f32x4 q[NT][NR];
+      typename F::Scales sc[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) sc[r] = F::scales(raw[r], g);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        u32x4 lo[NR], hi[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) F::weights(raw[r], sc[r], s, lo[r], hi[r]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const u32x4 x0 = *reinterpret_cast<const u32x4*>(xu + i * F::kXBytes + x_frag(s, g, col));
+          const u32x4 x1 = *reinterpret_cast<const u32x4*>(xu + i * F::kXBytes + x_frag(4 + s, g, col));
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            q[i][r] = mfma16(x0, lo[r], s == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : q[i][r]);
+            q[i][r] = mfma16(x1, hi[r], q[i][r]);
+          }
+        }
+        // the next unit's activations, and loads of the one after it
+#pragma unroll
+        for (int h = s * XG / 4; h < (s + 1) * XG / 4; ++h) {
+          store_x(u + 1, h);
+          load_x(u + 2, h);
+        }
+      }
+      store_sums(u + 1);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const u32x4 xsum = *reinterpret_cast<const u32x4*>(xu + i * F::kXBytes + x_frag(8, g, col));
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const f32x4 least = mfma16_bf(xsum, sc[r].mins, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            acc[i][r][v] = __builtin_fmaf(sc[r].d, q[i][r][v], __builtin_fmaf(-sc[r].dmin, least[v], acc[i][r][v]));
+        }
+      }
+      wait_vm<XG>();  // the copy (the activations' loads came after it)
+      read_w();
+      lds_barrier();
+    }
+  };
+  if (t.rows > BT / 2)
+    run(Int<TT>{});
+  else
+    run(Int<TT / 2>{});
+  wait_vm<0>();  // (no copy outlives the workgroup's LDS)
+#pragma unroll
+  for (int i = 0; i < TT; ++i)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int tok = 16 * i + 4 * g + v;
+      if (tok < t.rows) {
+        const int64_t at = (int64_t)(t.first + tok) * a.m + n0 + col;
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+          if (n0 + 16 * r + col < a.m) store_y(a.y, a.y_dtype, at + 16 * r, acc[i][r][v]);
+      }
+    }
+}
+
 // ---- many rows --------------------------------------------------------------------
 
 // Tile t of at most BT tokens times the 128 NB weight rows of `group`, on
@@ -618,8 +805,10 @@ __global__ __launch_bounds__(64 * kPfWaves, BT == 64 ? 2 : 1) void routed_tile_k
   routed_tile<F, BT, NB, XS>(a, t, group, xs0, xs1, xs2, ws0, ws1);
 }
 
+// FT: the format of routed_tile_kernel, or Q4kRows for routed_q4k_kernel.
 template <typename FR, typename FT>
 static hipError_t launch_routed(RoutedArgs a, hipStream_t s) {
+  constexpr bool kQ4k = std::is_same<FT, Q4kRows>::value;
   const int64_t used = a.n < a.e_count ? a.n : a.e_count, m = a.m;
   const int64_t rows = a.n / used;  // of a weight set, on average
   // tiles of bt tokens to expect: each weight set's last one is half full on average
@@ -628,8 +817,8 @@ static hipError_t launch_routed(RoutedArgs a, hipStream_t s) {
   };
   // What a kernel takes for 256 of K, in 1/100 us, by its workgroups: of 16 tokens
   // x 64 weight rows (K in parts while they are few, see below), 64 x 128 and 256 x 256
-  // (128 x 256 where weight sets have no more tokens).  Fitted to Q4_K, 8 weight
-  // sets of 14336 x 4096 (us measured by these three): 24 rows each 119, 126, -; 32
+  // (128 x 256 where weight sets have no more tokens).  Fitted to Q4_K through these three,
+  // 8 weight sets of 14336 x 4096 (us measured): 24 rows each 119, 126, -; 32
   // rows 145, 129, -; 50 rows -, 154, 167; 64 rows -, 190, 171; 64 sets of 1024 x 4096, 32
   // rows 88, 96, -.  Few weight rows leave large tiles a few CUs (TQ1_0, 102 rows of
   // one set of 13 x 13568: 21, -, 267; 5 sets of 726 x 9216, 362 rows: 99, -, 269).
@@ -638,8 +827,14 @@ static hipError_t launch_routed(RoutedArgs a, hipStream_t s) {
   const int64_t cost_few = few <= 128 ? 35 : few <= 256 ? 50 : 20 + 50 * few / 256;
   const int64_t cost_mid = 150 + 185 * std::max<int64_t>(mid, 256) / 256;
   const int64_t cost_big = (big + 255) / 256 * (rows <= 128 ? 530 : 760);
-  // (with at most 32 rows the weights are promised to enter as they are)
-  if (rows <= 32 || (cost_few <= cost_mid && cost_few <= cost_big)) {
+  // Q4_K's own, 64 x 256, one workgroup a CU (8 sets of 14336 x 4096, us by the first kernel
+  // and by this one: 12 rows each 76, 84; 16 rows 94, 82; 32 rows 140, 95; one set of 4096 x
+  // 4096: 256 rows 37, 46; 512 rows 66, 48; of 512 x 13568, 1600 rows: 108, 133).
+  const int64_t cost_q4k = (tiles(kQ4kBT) * ((m + kQ4kBN - 1) / kQ4kBN) + 255) / 256 * 270;
+  // Up to 32 rows a weight set the other formats' few-row kernel does better than the
+  // estimate, which is Q4_K's (8 sets of 14336 x 4096, 28 rows each: TQ1_0 91 us, 137 by
+  // tiles, NVFP4 119 and 132; 32 sets of 4096 x 4096, 32 rows each: 128, 141; 149, 138).
+  if (kQ4k ? cost_few <= cost_q4k : rows <= 32 || (cost_few <= cost_mid && cost_few <= cost_big)) {
     const auto go = [&](auto rw, auto kw) {
       constexpr int RW = decltype(rw)::value, KW = decltype(kw)::value;
       a.groups = (a.m + 16 * RW - 1) / (16 * RW);
@@ -660,14 +855,21 @@ static hipError_t launch_routed(RoutedArgs a, hipStream_t s) {
     if (few <= 256 || a.k > FR::kLongRows) return go(Int<4>{}, Int<2>{});
     return go(Int<4>{}, Int<1>{});
   }
-  const auto go = [&](auto btc, auto nbc) {
-    constexpr int BT = decltype(btc)::value, NB = decltype(nbc)::value;
-    a.groups = (a.m + kPfBN * NB - 1) / (kPfBN * NB);
-    hipLaunchKernelGGL((routed_tile_kernel<FT, BT, NB>), dim3((unsigned)(a.groups * max_tiles(a.n, a.e_count, BT))),
-                       dim3(64 * kPfWaves), 0, s, a);
+  if constexpr (kQ4k) {
+    a.groups = (a.m + kQ4kBN - 1) / kQ4kBN;
+    hipLaunchKernelGGL(routed_q4k_kernel, dim3((unsigned)(a.groups * max_tiles(a.n, a.e_count, kQ4kBT))),
+                       dim3(64 * kQ4kWaves), 0, s, a);
     return hipGetLastError();
-  };
-  return cost_mid <= cost_big ? go(Int<64>{}, Int<1>{}) : go(Int<256>{}, Int<2>{});
+  } else {
+    const auto go = [&](auto btc, auto nbc) {
+      constexpr int BT = decltype(btc)::value, NB = decltype(nbc)::value;
+      a.groups = (a.m + kPfBN * NB - 1) / (kPfBN * NB);
+      hipLaunchKernelGGL((routed_tile_kernel<FT, BT, NB>), dim3((unsigned)(a.groups * max_tiles(a.n, a.e_count, BT))),
+                         dim3(64 * kPfWaves), 0, s, a);
+      return hipGetLastError();
+    };
+    return cost_mid <= cost_big ? go(Int<64>{}, Int<1>{}) : go(Int<256>{}, Int<2>{});
+  }
 }
 
 hipError_t launch_routed(int fmt, const void* w, const void* x, const int32_t* order, const int32_t* offsets, void* y,
@@ -675,7 +877,7 @@ hipError_t launch_routed(int fmt, const void* w, const void* x, const int32_t* o
                          hipStream_t s) {
   const RoutedArgs a{static_cast<const uint8_t*>(w), static_cast<const uint16_t*>(x), order, offsets, y, expert_bytes,
                      (int)(t * choices), (int)choices, (int)e, (int)m, (int)k, (int)t, y_dtype, 0};
-  if (fmt == kRouteQ4k) return launch_routed<Q4kRows, Q4kPrefill>(a, s);
+  if (fmt == kRouteQ4k) return launch_routed<Q4kRows, Q4kRows>(a, s);
   if (fmt == kRouteNvfp4) return launch_routed<Nvfp4Rows, Nvfp4Prefill>(a, s);
   return launch_routed<Tq1Rows, Tq1Tile<true>>(a, s);
 }

@@ -91,11 +91,9 @@ int qroute_combine_grad(const void* dy, int32_t dy_dtype, const void* rows, int3
  *            order (the second).  x is fp16, for NVFP4 bf16.
  *   y        [T*k][M] of y_dtype, 16-byte aligned.  Rows that no weight set
  *            has are left as they were.
- * Sums are in fp32 and each output is rounded once to y_dtype.  With at most
- * 32 rows a weight set on average (T*k / min(E, T*k)) every weight enters as
- * it is; with more, Q4_K weights may be rounded once to fp16, as in the prefill
- * (qgemm_q4k), depending on the sizes alone; NVFP4 and TQ1_0 weights are exact
- * throughout.
+ * Sums are in fp32, each output is rounded once to y_dtype, and weights are never
+ * rounded: NVFP4's and TQ1_0's are exact in 16 bits, and Q4_K enters as
+ * d * sum(scale * q * x) - dmin * sum(min * x) over each block.
  * K as for the prefill (K <= 2^20, NVFP4 K % 64 == 0), M <= 2^24, and with
  * `order` x spans at most 2^30 bytes.  T == 0 or M == 0 is a no-op. */
 int qgemm_q4k_routed(const void* w, const void* x_f16, const int32_t* order, const int32_t* offsets, void* y,

@@ -136,10 +136,14 @@ __global__ __launch_bounds__(64 * kLoraDownWaves) void lora_down_kernel(LoraArgs
 // neighbouring columns of one token, and go through LDS to lanes that load c and
 // store y in whole lines (eight or sixteen lanes a row).
 //
-// v (with scale) is kept to fp32's precision: as three bf16 terms against
-// bf16 B (24 bits), and against fp16 B as two fp16 terms of v * 2^s, where s puts
-// the token's largest v in [2^14, 2^15) (22 bits or more of every v down to
-// 2^-28 of the largest; nothing over- or underflows), 2^-s going into the result.
+// v (with scale) is kept to fp32's precision: as three bf16 terms against bf16 B
+// (24 bits), and against fp16 B as three fp16 terms of v * 2^s, where s puts the
+// token's largest v in [2^14, 2^15) and each term holds, times 2^12, what the terms before
+// it leave over, and the terms' sums are joined by 2^-12 and 2^-s.  A term's smallest step
+// is 2^-24, the third's 2^-48 of v * 2^s: an fp32 v is held bit for bit down to
+// 2^-39 of the token's largest, and to 2^-63 of that below it.  (Two terms under one scale
+// hold 11 bits of a v of 2^-28 of the largest; 2048 tokens, r = 64, 14336 columns of fp16:
+// 47.5 us for the whole call, 49.3 with three.)
 //
 // 2048 tokens, 8 adapters of r = 64, 14336 columns of bf16: 37.8 us for 132 MB (3.5 TB/s),
 // fp32 55 us (4.5 TB/s).  Bound by c and y; before these went through LDS in whole
@@ -149,7 +153,7 @@ __global__ __launch_bounds__(64 * kLoraDownWaves) void lora_down_kernel(LoraArgs
 // Loose: rows of y are not whole dwords, or reach past 32-bit offsets.
 template <bool BF, typename TY, int TT, int RK, bool Loose, int RT = 0>
 __global__ __launch_bounds__(64 * (RT > 0 ? kLoraOneWaves : kLoraUpWaves)) void lora_up_kernel(LoraArgs g) {
-  constexpr int BT = 16 * TT, NW = RT > 0 ? kLoraOneWaves : kLoraUpWaves, kTerms = BF ? 3 : 2;
+  constexpr int BT = 16 * TT, NW = RT > 0 ? kLoraOneWaves : kLoraUpWaves, kTerms = 3;
   constexpr int U = RT == 1 ? 4 : RT == 2 ? 2 : 1;
   static_assert(RT == 0 || TT == 1, "one tile of 16 tokens");
   // c and y in pieces of 16 bytes
@@ -322,9 +326,9 @@ __global__ __launch_bounds__(64 * (RT > 0 ? kLoraOneWaves : kLoraUpWaves)) void 
   if constexpr (!BF) {
 #pragma unroll
     for (int m = kLanes / 2; m >= 1; m >>= 1) top = __builtin_fmaxf(top, shfl_xor(top, m));
-    // (a row of zeros keeps its scale; infinities and NaN do not count)
+    // (infinities and NaN do not count)
     const int ex = (int)((__builtin_bit_cast(unsigned, top) >> 23) & 255) - 127;
-    const int sh = ex == -127 ? 0 : min(max(14 - ex, -126), 126);
+    const int sh = min(14 - ex, 126);  // at least -113
     up = __builtin_bit_cast(float, (unsigned)(127 + sh) << 23);
     if (in == 0) undo[tok] = __builtin_bit_cast(float, (unsigned)(127 - sh) << 23);
   }
@@ -343,7 +347,7 @@ __global__ __launch_bounds__(64 * (RT > 0 ? kLoraOneWaves : kLoraUpWaves)) void 
             rest = (b[l] & 0x7FFF) == 0x7F80 ? 0.f : rest - (float)__builtin_bit_cast(__bf16, b[l]);
           } else {
             b[l] = __builtin_bit_cast(unsigned short, (_Float16)rest);
-            rest = (b[l] & 0x7FFF) == 0x7C00 ? 0.f : rest - (float)__builtin_bit_cast(_Float16, b[l]);
+            rest = (b[l] & 0x7FFF) == 0x7C00 ? 0.f : (rest - (float)__builtin_bit_cast(_Float16, b[l])) * 4096.f;
           }
           v[i][l] = rest;
         }
@@ -357,30 +361,53 @@ __global__ __launch_bounds__(64 * (RT > 0 ? kLoraOneWaves : kLoraUpWaves)) void 
   const auto one_group = [&](int grp, const Ahead& now, Ahead& next) {
     load_ahead(grp + step, next);
     __builtin_amdgcn_sched_barrier(0);  // (the compiler would put them off until after the products)
-    f32x4 acc[TT][4];
+    // fp16: the terms' sums are joined smallest first, each scaled to the next term.
+    // With B in registers the terms are taken one after the other through one sum; B
+    // that is loaded as it goes is loaded once, with a sum for each term (r = 128, 2048
+    // tokens, 4096 columns: B loaded three times 57 us, three sums 38).
+    constexpr int kSums = !BF && RK == 0 ? kTerms : 1;
+    f32x4 acc[kSums][TT][4];
 #pragma unroll
-    for (int u = 0; u < TT; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[u][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const auto multiply = [&](int k0, const u32x4 (&f)[4]) {
+    for (int k = 0; k < kSums; ++k)
 #pragma unroll
       for (int u = 0; u < TT; ++u)
 #pragma unroll
-        for (int k = 0; k < kTerms; ++k) {
-          const u32x4 vf = *reinterpret_cast<const u32x4*>(vs + (k * BT + 16 * u + col) * stride + k0 + 8 * q);
+        for (int i = 0; i < 4; ++i) acc[k][u][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const auto multiply = [&](int term, int k0, const u32x4 (&f)[4]) {
+      auto& sum = acc[kSums > 1 ? term : 0];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[u][i] = lora_mfma<BF>(f[i], vf, acc[u][i]);
-        }
+      for (int u = 0; u < TT; ++u) {
+        const u32x4 vf = *reinterpret_cast<const u32x4*>(vs + (term * BT + 16 * u + col) * stride + k0 + 8 * q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[u][i] = lora_mfma<BF>(f[i], vf, sum[u][i]);
+      }
     };
     if constexpr (RK > 0) {
 #pragma unroll
-      for (int k = 0; k < RK; ++k) multiply(32 * k, now.b[k]);
+      for (int term = kTerms - 1; term >= 0; --term) {
+#pragma unroll
+        for (int k = 0; k < RK; ++k) multiply(term, 32 * k, now.b[k]);
+        if (!BF && term > 0)
+#pragma unroll
+          for (int u = 0; u < TT; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[0][u][i] *= 0x1p-12f;
+      }
     } else {
       for (int k0 = 0; k0 < rp; k0 += 32) {
         u32x4 f[4];
         load_b(grp, k0, f);
-        multiply(k0, f);
+#pragma unroll
+        for (int term = 0; term < kTerms; ++term) multiply(term, k0, f);
       }
+      if constexpr (kSums > 1)
+#pragma unroll
+        for (int u = 0; u < TT; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[0][u][i][j] = __builtin_fmaf(__builtin_fmaf(acc[2][u][i][j], 0x1p-12f, acc[1][u][i][j]), 0x1p-12f, acc[0][u][i][j]);
     }
     // granule i of a row of 16 sits at i ^ row: no bank conflicts
 #pragma unroll
@@ -388,7 +415,7 @@ __global__ __launch_bounds__(64 * (RT > 0 ? kLoraOneWaves : kLoraUpWaves)) void 
       const float un = BF ? 1.f : undo[16 * u + col];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<f32x4*>(mine + (16 * u + col) * 64 + 4 * ((4 * i + q) ^ col)) = acc[u][i] * un;
+        *reinterpret_cast<f32x4*>(mine + (16 * u + col) * 64 + 4 * ((4 * i + q) ^ col)) = acc[0][u][i] * un;
     }
     compiler_fence();
     __builtin_amdgcn_wave_barrier();
@@ -457,7 +484,7 @@ static hipError_t with_y(const LoraArgs& g, F&& f) {
 
 template <bool BF>
 static hipError_t launch_lora(LoraArgs g, const LoraPlan& p, hipStream_t s) {
-  const size_t row_lds = (size_t)(BF ? 3 : 2) * ((g.r + 31) / 32 * 32 + 8) * 2;  // bytes of a token's v
+  const size_t row_lds = (size_t)3 * ((g.r + 31) / 32 * 32 + 8) * 2;  // bytes of a token's v
   // One launch where it takes at most a workgroup a CU and reading the adapter's
   // whole A in each of them costs less than the second launch: r is small (24
   // tokens, r = 16, 4096 x 4096: at the time 9.0 us of GPU time against 8.4 with two, but

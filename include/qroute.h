@@ -121,7 +121,9 @@ int qgemm_tq1_routed(const void* w, const void* x_f16, const int32_t* order, con
  *   workspace  qlora_workspace_bytes(T, E, r, M, K) bytes, 256-byte aligned;
  *            contents need no initialisation and are overwritten, so calls
  *            that overlap in time must not share it.
- * A_e x[t] is kept in fp32 and the sum is rounded once to y_dtype.
+ * A_e x[t] is kept in fp32 (qlora_f16: bit for bit down to 2^-39 of the token's
+ * largest component, smaller ones to 2^-63 of it) and the sum is rounded once to
+ * y_dtype.  An infinite element of b gives NaN.
  * 0 < r <= 256, r % 8 == 0; K % 8 == 0, K <= 2^20; M <= 2^24; x spans at most
  * 2^30 bytes.  T == 0 or M == 0 is a no-op. */
 int64_t qlora_workspace_bytes(int64_t T, int64_t E, int64_t r, int64_t M, int64_t K);

@@ -21,7 +21,7 @@ int check_rows(int64_t t, int64_t k, int64_t c) {
   const int rc = check_slots(t, k);
   if (rc != QGEMV_OK) return rc;
   if (c < 0 || c > kMaxK) return QGEMV_E_SHAPE;
-  if (t * k * c > kRouteMaxElems) return QGEMV_E_SHAPE;
+  if (t * k * (c + 16) > kRouteMaxElems) return QGEMV_E_SHAPE;
   return QGEMV_OK;
 }
 
@@ -33,8 +33,7 @@ int gemm_routed(Fmt f, RouteFmt rf, const void* w, const void* x, const int32_t*
   if (e < 1 || e > QROUTE_MAX_E || m > kMaxK || kk > kPrefillMaxK) return QGEMV_E_SHAPE;
   if (f == kNvfp4 && kk % 64 != 0) return QGEMV_E_SHAPE;  // whole 64-weight steps
   const int64_t n = t * k;
-  // one workgroup for at least 16 weight rows and a tile of at most 16 slots of one weight set
-  if ((m + 15) / 16 * ((n < e ? n : e) + n / 16) > kMaxM) return QGEMV_E_SHAPE;
+  if (n > 0 && m > 0 && routed_work_items(routed_plan(rf, n, e, m, kk)) > kMaxWorkItems) return QGEMV_E_SHAPE;
   if (order && t * kk * 2 > kRouteMaxXBytes) return QGEMV_E_SHAPE;
   if (!valid_dtype(y_dtype)) return QGEMV_E_DTYPE;
   if (t == 0 || m == 0) return QGEMV_OK;

@@ -5,14 +5,13 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "route_grid.hpp"
+
 namespace qgemv {
 
 int64_t route_sort_workspace(int64_t n, int64_t e);
 hipError_t launch_route_sort(const int32_t* ids, int64_t n, int64_t e, int32_t* order, int32_t* position,
                              int32_t* offsets, void* ws, hipStream_t s);
-// Elements of the rows that one call of the row movers takes at most (one thread for
-// each piece of 8, in workgroups of 256).
-constexpr int64_t kRouteMaxElems = int64_t(1) << 38;
 hipError_t launch_route_gather(const void* x, const int32_t* order, const float* weights, void* out, int dtype,
                                int64_t t, int64_t k, int64_t c, hipStream_t s);
 hipError_t launch_route_combine(const void* rows, int rows_dtype, const int32_t* position, const float* weights,
@@ -21,8 +20,6 @@ hipError_t launch_route_combine_grad(const void* dy, int dy_dtype, const void* r
                                      const int32_t* position, const float* weights, void* drows, float* dweights,
                                      int64_t t, int64_t k, int64_t c, hipStream_t s);
 
-// Routed products on packed matrices of format `fmt`.
-enum RouteFmt : int { kRouteQ4k = 0, kRouteNvfp4 = 1, kRouteTq1 = 2 };
 // Largest span of the activations that a plan's rows are picked from.
 constexpr int64_t kRouteMaxXBytes = int64_t(1) << 30;
 hipError_t launch_routed(int fmt, const void* w, const void* x, const int32_t* order, const int32_t* offsets, void* y,

@@ -482,6 +482,9 @@ static hipError_t with_y(const LoraArgs& g, F&& f) {
   return f(__bf16{}, Int<0>{});
 }
 
+// Work items: at most 2^20 + 2^10 tiles of 16 tokens (t <= 2^24, e <= 1024) times 4 pieces
+// of r times 512 threads for the first product, parts of K and chunks of m only while
+// tiles are few: below 2^32.
 template <bool BF>
 static hipError_t launch_lora(LoraArgs g, const LoraPlan& p, hipStream_t s) {
   const size_t row_lds = (size_t)3 * ((g.r + 31) / 32 * 32 + 8) * 2;  // bytes of a token's v

@@ -247,7 +247,7 @@ struct Piece {
   int at, count;
 };
 template <bool Loose>
-__host__ __device__ __forceinline__ int row_pieces(int c) {
+__device__ __forceinline__ int row_pieces(int c) {  // route_row_pieces
   return (c + 7) / 8 + (Loose ? 1 : 0);
 }
 template <bool Loose>
@@ -391,11 +391,6 @@ template <typename F>
 static hipError_t with_rows(int64_t c, F&& f) {
   return c % 8 == 0 ? f(Int<0>{}) : f(Int<1>{});
 }
-template <bool Loose>
-static unsigned piece_grid(int64_t rows, int64_t c) {
-  return (unsigned)((rows * row_pieces<Loose>((int)c) + 255) / 256);
-}
-
 hipError_t launch_route_gather(const void* x, const int32_t* order, const float* weights, void* out, int dtype,
                                int64_t t, int64_t k, int64_t c, hipStream_t s) {
   const int64_t n = t * k;
@@ -403,7 +398,7 @@ hipError_t launch_route_gather(const void* x, const int32_t* order, const float*
     typedef decltype(type) T;
     return with_rows(c, [&](auto lc) {
       constexpr bool Loose = decltype(lc)::value != 0;
-      const dim3 grid(piece_grid<Loose>(n, c));
+      const dim3 grid((unsigned)route_move_workgroups(n, c));
       if (weights)
         hipLaunchKernelGGL((route_gather_kernel<T, Loose, true>), grid, dim3(256), 0, s, (const T*)x, order, weights,
                            (T*)out, n, (int)k, (int)c, t * c);
@@ -423,7 +418,7 @@ hipError_t launch_route_combine(const void* rows, int rows_dtype, const int32_t*
       typedef decltype(yt) TY;
       return with_rows(c, [&](auto lc) {
         constexpr bool Loose = decltype(lc)::value != 0;
-        hipLaunchKernelGGL((route_combine_kernel<TR, TY, Loose>), dim3(piece_grid<Loose>(t, c)), dim3(256), 0, s,
+        hipLaunchKernelGGL((route_combine_kernel<TR, TY, Loose>), dim3((unsigned)route_move_workgroups(t, c)), dim3(256), 0, s,
                            (const TR*)rows, position, weights, (TY*)y, t, (int)k, (int)c);
         return hipGetLastError();
       });
@@ -442,13 +437,12 @@ hipError_t launch_route_combine_grad(const void* dy, int dy_dtype, const void* r
         constexpr bool Loose = decltype(lc)::value != 0;
         const auto go = [&](auto kc, auto wc) {
           constexpr int KJ = decltype(kc)::value, W = decltype(wc)::value;
-          hipLaunchKernelGGL((route_combine_grad_kernel<TD, TR, Loose, KJ, W>), dim3((unsigned)((t + 4 / W - 1) / (4 / W))),
+          hipLaunchKernelGGL((route_combine_grad_kernel<TD, TR, Loose, KJ, W>), dim3((unsigned)route_grad_workgroups(t, c)),
                              dim3(256), 0, s, (const TD*)dy, (const TR*)rows, position, weights, (TR*)drows, dweights,
                              t, (int)k, (int)c);
           return hipGetLastError();
         };
-        // rows of at most 1024 elements are one wave's
-        const auto waves = [&](auto kc) { return c <= 1024 ? go(kc, Int<1>{}) : go(kc, Int<4>{}); };
+        const auto waves = [&](auto kc) { return route_grad_waves(t, c) == 1 ? go(kc, Int<1>{}) : go(kc, Int<4>{}); };
         return k <= 2 ? waves(Int<2>{}) : waves(Int<4>{});
       });
     });

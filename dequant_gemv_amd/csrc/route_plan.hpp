@@ -5,6 +5,7 @@
 #include "device.hpp"
 #include "epilogue.hpp"
 #include "prefill_tile.hpp"
+#include "route_grid.hpp"
 
 namespace qgemv {
 
@@ -58,12 +59,6 @@ __device__ __forceinline__ RoutedTile find_tile(const int32_t* offsets, int e_co
     carry += __shfl(incl, 63);
   }
   return RoutedTile{0, 0, 0};
-}
-
-// Tiles of bt rows that n slots over e weight sets can make at most.
-inline int64_t max_tiles(int64_t n, int64_t e, int64_t bt) {
-  const int64_t used = n < e ? n : e;
-  return used + (n - used) / bt;
 }
 
 // Workgroup b of n as its place in a walk that gives each of the eight XCDs (b %

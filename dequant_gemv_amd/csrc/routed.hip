@@ -2,7 +2,7 @@
 // that a plan (include/qroute.h) gives to each weight set e, on packed Q4_K,
 // NVFP4 and TQ1_0 matrices.
 //
-// Kernels, chosen by the number of rows and tiles (launch_routed):
+// Kernels, chosen by the number of rows and tiles (routed_plan):
 //  - few rows (decode), or too few tiles for the CUs: every wave streams its own
 //    weight rows through LDS and decodes them straight into matrix-core operands,
 //    once per 16 rows (routed_rows_kernel);
@@ -12,7 +12,6 @@
 //  - many rows of Q4_K, whose weights are not (a 16-bit weight is off by up to 2^-11
 //    of itself): the first kernel's arithmetic with 64 tokens a workgroup
 //    (routed_q4k_kernel).
-#include <algorithm>
 #include <type_traits>
 
 #include "device.hpp"
@@ -125,7 +124,6 @@ __device__ __forceinline__ unsigned bf16_bits(float v) {
 // its lane, against min_g (6 bits, exact).
 struct Q4kRows {
   static constexpr int kUnit = 256;
-  static constexpr int kLongRows = 1 << 24;  // see launch_routed
   static constexpr bool kWholeUnits = true;
   struct X {
     u32x4 f[8];
@@ -262,7 +260,6 @@ struct Q4kRows {
 // |scale| is exact in bf16.
 struct Nvfp4Rows {
   static constexpr int kUnit = 256;
-  static constexpr int kLongRows = 1 << 24;
   static constexpr bool kWholeUnits = false;
   struct X {
     u32x4 f[8];
@@ -348,7 +345,6 @@ struct Nvfp4Rows {
 // exact in fp16 and d is applied to the fp32 sums of the block.
 struct Tq1Rows {
   static constexpr int kUnit = 256;
-  static constexpr int kLongRows = 8192;
   static constexpr bool kWholeUnits = true;
   struct X {
     u32x4 f[8];
@@ -589,10 +585,6 @@ __global__ __launch_bounds__(64 * RW * KW, RW * KW == 4 ? 3 : 2) void routed_row
 // sets took 115 to 160 us, 82 to 140 like this.  Tiles of 96 tokens: 719 us, but 128 us
 // against 101 for 512 rows of one set; 48 weight rows a wave: 728, 133; 16 waves of 16
 // rows: 788, 104.
-constexpr int kQ4kBT = 64;   // tokens of a workgroup
-constexpr int kQ4kBN = 256;  // its weight rows
-constexpr int kQ4kWaves = 8;
-
 __global__ __launch_bounds__(64 * kQ4kWaves, 2) void routed_q4k_kernel(RoutedArgs a) {
   typedef Q4kRows F;
   constexpr int BT = kQ4kBT, TT = BT / 16, RW = kQ4kWaves, NR = kQ4kBN / (16 * RW);
@@ -805,71 +797,29 @@ __global__ __launch_bounds__(64 * kPfWaves, BT == 64 ? 2 : 1) void routed_tile_k
   routed_tile<F, BT, NB, XS>(a, t, group, xs0, xs1, xs2, ws0, ws1);
 }
 
-// FT: the format of routed_tile_kernel, or Q4kRows for routed_q4k_kernel.
 template <typename FR, typename FT>
-static hipError_t launch_routed(RoutedArgs a, hipStream_t s) {
-  constexpr bool kQ4k = std::is_same<FT, Q4kRows>::value;
-  const int64_t used = a.n < a.e_count ? a.n : a.e_count, m = a.m;
-  const int64_t rows = a.n / used;  // of a weight set, on average
-  // tiles of bt tokens to expect: each weight set's last one is half full on average
-  const auto tiles = [&](int64_t bt) {
-    return used == 1 ? (a.n + bt - 1) / bt : std::max<int64_t>(used, a.n / bt + used / 2);
-  };
-  // What a kernel takes for 256 of K, in 1/100 us, by its workgroups: of 16 tokens
-  // x 64 weight rows (K in parts while they are few, see below), 64 x 128 and 256 x 256
-  // (128 x 256 where weight sets have no more tokens).  Fitted to Q4_K through these three,
-  // 8 weight sets of 14336 x 4096 (us measured): 24 rows each 119, 126, -; 32
-  // rows 145, 129, -; 50 rows -, 154, 167; 64 rows -, 190, 171; 64 sets of 1024 x 4096, 32
-  // rows 88, 96, -.  Few weight rows leave large tiles a few CUs (TQ1_0, 102 rows of
-  // one set of 13 x 13568: 21, -, 267; 5 sets of 726 x 9216, 362 rows: 99, -, 269).
-  const int64_t few = tiles(16) * ((m + 63) / 64), mid = tiles(64) * ((m + 127) / 128);
-  const int64_t big = tiles(256) * ((m + 255) / 256);
-  const int64_t cost_few = few <= 128 ? 35 : few <= 256 ? 50 : 20 + 50 * few / 256;
-  const int64_t cost_mid = 150 + 185 * std::max<int64_t>(mid, 256) / 256;
-  const int64_t cost_big = (big + 255) / 256 * (rows <= 128 ? 530 : 760);
-  // Q4_K's own, 64 x 256, one workgroup a CU (8 sets of 14336 x 4096, us by the first kernel
-  // and by this one: 12 rows each 76, 84; 16 rows 94, 82; 32 rows 140, 95; one set of 4096 x
-  // 4096: 256 rows 37, 46; 512 rows 66, 48; of 512 x 13568, 1600 rows: 108, 133).
-  const int64_t cost_q4k = (tiles(kQ4kBT) * ((m + kQ4kBN - 1) / kQ4kBN) + 255) / 256 * 270;
-  // Up to 32 rows a weight set the other formats' few-row kernel does better than the
-  // estimate, which is Q4_K's (8 sets of 14336 x 4096, 28 rows each: TQ1_0 91 us, 137 by
-  // tiles, NVFP4 119 and 132; 32 sets of 4096 x 4096, 32 rows each: 128, 141; 149, 138).
-  if (kQ4k ? cost_few <= cost_q4k : rows <= 32 || (cost_few <= cost_mid && cost_few <= cost_big)) {
-    const auto go = [&](auto rw, auto kw) {
-      constexpr int RW = decltype(rw)::value, KW = decltype(kw)::value;
-      a.groups = (a.m + 16 * RW - 1) / (16 * RW);
-      hipLaunchKernelGGL((routed_rows_kernel<FR, RW, KW>), dim3((unsigned)(a.groups * max_tiles(a.n, a.e_count, 16))),
-                         dim3(64 * RW * KW), 0, s, a);
-      return hipGetLastError();
-    };
-    // Workgroups of 64 rows and all of K where that gives more than a CU's one
-    // (three fit a CU).  With fewer, a workgroup's walk through K is what takes
-    // the time: 64 rows with K in two parts, or 32 with K in four, while these
-    // make at most one workgroup a CU (Q4_K, one token, two weight sets: 14336 x
-    // 4096 15.3 / 19.1 / 28.6 us in this order, 8192 x 4096 12.0 / 10.8 / 15.5,
-    // 4096 x 4096 11.6 / 11.1 / 9.3, 4096 x 14336 30.6 / 28.4 / 17.7).
-    if (few <= 128) return go(Int<2>{}, Int<4>{});
-    // (TQ1_0, whose decoding takes longer than its few bytes, also for long rows:
-    // 74 slots over 8 weight sets of 4096 x 14336, at the time 60 us with two parts,
-    // 70 with one or with four, 64 with 128 rows and two parts)
-    if (few <= 256 || a.k > FR::kLongRows) return go(Int<4>{}, Int<2>{});
-    return go(Int<4>{}, Int<1>{});
-  }
-  if constexpr (kQ4k) {
-    a.groups = (a.m + kQ4kBN - 1) / kQ4kBN;
-    hipLaunchKernelGGL(routed_q4k_kernel, dim3((unsigned)(a.groups * max_tiles(a.n, a.e_count, kQ4kBT))),
-                       dim3(64 * kQ4kWaves), 0, s, a);
+static hipError_t launch_routed(int fmt, RoutedArgs a, hipStream_t s) {
+  const RoutedPlan p = routed_plan(fmt, a.n, a.e_count, a.m, a.k);
+  a.groups = (int)p.groups;
+  const dim3 grid((unsigned)(p.groups * p.tiles)), block((unsigned)p.threads);
+  const auto rows = [&](auto rw, auto kw) {
+    hipLaunchKernelGGL((routed_rows_kernel<FR, decltype(rw)::value, decltype(kw)::value>), grid, block, 0, s, a);
     return hipGetLastError();
+  };
+  if (p.kernel == kRoutedRows)
+    return p.rw == 2   ? rows(Int<2>{}, Int<4>{})
+           : p.kw == 2 ? rows(Int<4>{}, Int<2>{})
+                       : rows(Int<4>{}, Int<1>{});
+  if constexpr (std::is_same<FT, Q4kRows>::value) {
+    hipLaunchKernelGGL(routed_q4k_kernel, grid, block, 0, s, a);
   } else {
-    const auto go = [&](auto btc, auto nbc) {
-      constexpr int BT = decltype(btc)::value, NB = decltype(nbc)::value;
-      a.groups = (a.m + kPfBN * NB - 1) / (kPfBN * NB);
-      hipLaunchKernelGGL((routed_tile_kernel<FT, BT, NB>), dim3((unsigned)(a.groups * max_tiles(a.n, a.e_count, BT))),
-                         dim3(64 * kPfWaves), 0, s, a);
-      return hipGetLastError();
-    };
-    return cost_mid <= cost_big ? go(Int<64>{}, Int<1>{}) : go(Int<256>{}, Int<2>{});
+    static_assert(kPfWaves == 8, "threads of a tile's workgroup");
+    if (p.bt == 64)
+      hipLaunchKernelGGL((routed_tile_kernel<FT, 64, 1>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((routed_tile_kernel<FT, 256, 2>), grid, block, 0, s, a);
   }
+  return hipGetLastError();
 }
 
 hipError_t launch_routed(int fmt, const void* w, const void* x, const int32_t* order, const int32_t* offsets, void* y,
@@ -877,9 +827,9 @@ hipError_t launch_routed(int fmt, const void* w, const void* x, const int32_t* o
                          hipStream_t s) {
   const RoutedArgs a{static_cast<const uint8_t*>(w), static_cast<const uint16_t*>(x), order, offsets, y, expert_bytes,
                      (int)(t * choices), (int)choices, (int)e, (int)m, (int)k, (int)t, y_dtype, 0};
-  if (fmt == kRouteQ4k) return launch_routed<Q4kRows, Q4kRows>(a, s);
-  if (fmt == kRouteNvfp4) return launch_routed<Nvfp4Rows, Nvfp4Prefill>(a, s);
-  return launch_routed<Tq1Rows, Tq1Tile<true>>(a, s);
+  if (fmt == kRouteQ4k) return launch_routed<Q4kRows, Q4kRows>(fmt, a, s);
+  if (fmt == kRouteNvfp4) return launch_routed<Nvfp4Rows, Nvfp4Prefill>(fmt, a, s);
+  return launch_routed<Tq1Rows, Tq1Tile<true>>(fmt, a, s);
 }
 
 }  // namespace qgemv

@@ -22,7 +22,9 @@
  * on the host: entries that no qroute_sort writes (positions, slots or offsets
  * outside their ranges) never lead to an access outside the arrays, and give
  * unspecified values.  All results are the same bits on every run.
- * Limits: k <= 64, E <= 1024, n <= 2^24.
+ * Limits: k <= 64, E <= 1024, n <= 2^24; the row movers take T*k*(C + 16) <= 2^35.
+ * A product whose launch would take 2^32 work items or more is QGEMV_E_SHAPE: none does
+ * while ceil(M / 64) * (T*k / 16 + min(T*k, E)) < 2^23.
  */
 #ifndef QROUTE_H
 #define QROUTE_H

@@ -13,7 +13,6 @@
 namespace qgemv {
 
 typedef unsigned u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
-typedef unsigned u32x3_a4 __attribute__((ext_vector_type(3), aligned(4)));
 
 // N elements as their bits: 8 of any type, or 4 of fp32.
 template <typename T, int N = 8>
@@ -106,7 +105,7 @@ __device__ __forceinline__ void store_bits(T* p, int64_t e, int count, const Bit
     if (rest == 8) {
       *reinterpret_cast<u32x4_a4*>(to) = u32x4_a4{w[0], w[1], w[2], w[3]};
     } else if (rest == 7) {
-      *reinterpret_cast<u32x3_a4*>(to) = u32x3_a4{w[0], w[1], w[2]};
+      __builtin_memcpy(to, w, 12);  // (a vector of three has the size of four, and a store of it may have too)
     } else {
 #pragma unroll
       for (int i = 0; i < 3; ++i)

@@ -60,12 +60,12 @@ __device__ __forceinline__ Bits<T, N> load_bits(const T* p, int64_t e, int count
       for (int j = 0; j < 4; ++j) b.w[4 * i + j] = 4 * i + j < count ? v[j] : 0u;
     }
   } else {
-    // the dwords that hold the 16 bytes; the fifth only where the piece starts in
-    // the middle of one (its first half is then the piece's last element)
+    // the dwords that hold the 16 bytes; where the piece starts in the middle of
+    // one, its last element is the first half of a fifth, whose other half may be past the array
     const unsigned* const src = reinterpret_cast<const unsigned*>(p) + (e >> 1);
     const u32x4_a4 v = *reinterpret_cast<const u32x4_a4*>(src);
     const unsigned odd = (unsigned)e & 1u;
-    const unsigned last = odd ? src[4] : 0u;
+    const unsigned last = odd ? (unsigned)reinterpret_cast<const uint16_t*>(p)[e + 7] : 0u;
     b.w[0] = __builtin_amdgcn_alignbyte(v[1], v[0], 2u * odd);
     b.w[1] = __builtin_amdgcn_alignbyte(v[2], v[1], 2u * odd);
     b.w[2] = __builtin_amdgcn_alignbyte(v[3], v[2], 2u * odd);

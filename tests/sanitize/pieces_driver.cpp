@@ -1,6 +1,6 @@
 // Loads and stores of row pieces (csrc/pieces.hpp) on the host, under
 // AddressSanitizer: every piece of arrays of every length ending at any element, from
-// buffers that hold the array and nothing more (to be read: whole dwords).  The device builtins and helpers that
+// buffers that hold the array and nothing more.  The device builtins and helpers that
 // pieces.hpp takes from its neighbours are replaced by the host forms in device.hpp
 // beside this file's copy.  Exits non-zero on the first mismatch.
 #include <stdio.h>
@@ -17,7 +17,7 @@ template <typename T, int N>
 static void check(const char* what) {
   for (int64_t total = 1; total <= 41; ++total) {
     const size_t bytes = total * sizeof(T);
-    unsigned char* const src = static_cast<unsigned char*>(malloc((bytes + 3) / 4 * 4));  // (16-byte aligned)
+    unsigned char* const src = static_cast<unsigned char*>(malloc(bytes));  // (16-byte aligned)
     unsigned char* const dst = static_cast<unsigned char*>(malloc(bytes));  // (16-byte aligned)
     for (size_t i = 0; i < bytes; ++i) src[i] = (unsigned char)(37 * i + 11);
     for (int64_t e = 0; e < total; ++e)

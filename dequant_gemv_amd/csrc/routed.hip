@@ -352,6 +352,8 @@ struct Tq1Rows {
   struct Desc {
     __amdgpu_buffer_rsrc_t r;
     uint32_t lead;
+    int last;               // the last row
+    unsigned short last_d;  // and its last block's d
   };
   struct Raw {
     // the dwords that hold qs bytes 4 g .. + 4, 16 + 4 g .. + 4 and 32 + 4 g .. + 4, and the qh bytes
@@ -363,7 +365,9 @@ struct Tq1Rows {
     const uint32_t rb = (uint32_t)(k / 256 * 54);
     const uint8_t* const first = w + (int64_t)n0 * rb;
     const uint32_t lead = (uint32_t)reinterpret_cast<uintptr_t>(first) & 3u;
-    return Desc{make_rsrc(first - lead, nv > 0 ? ((uint32_t)nv * rb + lead + 3u) & ~3u : 0u), lead};
+    const uint32_t bytes = (uint32_t)nv * rb;
+    return Desc{make_rsrc(first - lead, nv > 0 ? (bytes + lead) & ~3u : 0u), lead, nv - 1,
+                ld16(make_rsrc(first, bytes), bytes - 2u)};
   }
   static __device__ __forceinline__ uint32_t row_offset(int k, int r) { return (uint32_t)r * (uint32_t)(k / 256 * 54); }
   // fp16 codes of digit - 1 of the two bytes in the halves of l; l moves to the next digit
@@ -404,9 +408,8 @@ struct Tq1Rows {
 
   // Staged: two units of 16 rows, per row the 112 bytes from the dword at or
   // below the two blocks' first byte (108 bytes and up to 2 before them), which
-  // 16 rows put in 16 different bank groups.  The descriptor ends at the dword
-  // that holds the last row's last byte, since a dword partly past the end reads
-  // as zero.
+  // 16 rows put in 16 different bank groups.  A dword partly past the last row's end
+  // is not read (the matrix may end there), and the d in it is loaded by itself.
   static constexpr int kStageUnits = 2;
   static constexpr int kXBytes = 8 * 1024;  // eight operands
   static constexpr int kCopies = 2;
@@ -426,7 +429,7 @@ struct Tq1Rows {
   static __device__ __forceinline__ void copy(const Desc& d, const Staged& st, unsigned char* lds, int stage, bool live) {
     copy_chunks<112>(d.r, lds, st.at, 108u * (uint32_t)stage, live);
   }
-  static __device__ __forceinline__ Raw read(const Desc& d, const unsigned char* lds, int unit, int row, int g, int,
+  static __device__ __forceinline__ Raw read(const Desc& d, const unsigned char* lds, int unit, int row, int g, int u,
                                              int k) {
     const uint32_t blk = ((d.lead + row_offset(k, row)) & 2u) + 54u * (uint32_t)unit;  // in the row's 112 bytes
     const unsigned char* const b = lds + 112 * row + (blk & ~3u);
@@ -436,7 +439,8 @@ struct Tq1Rows {
     r.a1 = u32x2{dword(16 + 4 * g), dword(20 + 4 * g)};
     r.b = u32x2{dword(32 + 4 * g), dword(36 + 4 * g)};
     r.c = u32x2{dword(48), dword(52)};
-    r.d = *reinterpret_cast<const unsigned short*>(lds + 112 * row + blk + 52);
+    const unsigned short own = *reinterpret_cast<const unsigned short*>(lds + 112 * row + blk + 52);
+    r.d = row == (u == k / 256 - 1 ? d.last : -1) ? d.last_d : own;
     r.shift = blk & 3u;
     return r;
   }

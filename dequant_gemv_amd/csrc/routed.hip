@@ -123,6 +123,7 @@ __device__ __forceinline__ unsigned bf16_bits(float v) {
 // one bf16 MFMA, X_g split into three bf16 terms (24 bits) in the K slots of
 // its lane, against min_g (6 bits, exact).
 struct Q4kRows {
+  static constexpr bool kDefinition = true;
   static constexpr int kUnit = 256;
   static constexpr bool kWholeUnits = true;
   struct X {
@@ -192,6 +193,27 @@ struct Q4kRows {
     lo = u32x4{low(b0), low(b0 >> 8), low(b1), low(b1 >> 8)};
     hi = u32x4{high(b0), high(b0 >> 8), high(b1), high(b1 >> 8)};
   }
+  // One output by the definition, sum of (d * scale * q - dmin * min) * x.
+  static __device__ __forceinline__ float definition(const uint8_t* row, const uint16_t* x, int k) {
+    float sum = 0.f;
+    for (int b = 0; b < k / 256; ++b) {
+      const uint8_t* const blk = row + 144 * (int64_t)b;
+      const u32x4 hdr = *reinterpret_cast<const u32x4*>(blk);
+      const float d = f16lo(hdr.x), dmin = f16hi(hdr.x);
+      for (int g = 0; g < 8; ++g) {
+        const unsigned sh = 8u * (unsigned)(g & 3), lo = hdr.y >> sh, mid = hdr.z >> sh, hi = hdr.w >> sh;
+        const unsigned sc = g < 4 ? lo & 63u : (hi & 15u) | ((lo >> 2) & 48u);
+        const unsigned mn = g < 4 ? mid & 63u : ((hi >> 4) & 15u) | ((mid >> 2) & 48u);
+        const float ds = d * (float)sc, least = dmin * (float)mn;
+        for (int i = 0; i < 32; ++i) {
+          const unsigned q = ((unsigned)blk[16 + 32 * (g >> 1) + i] >> (4 * (g & 1))) & 15u;
+          const float v = (float)__builtin_bit_cast(_Float16, x[256 * b + 32 * g + i]);
+          sum = __builtin_fmaf(__builtin_fmaf(ds, (float)q, -least), v, sum);
+        }
+      }
+    }
+    return sum;
+  }
   static __device__ __forceinline__ void mma(const Raw& raw, const X& x, int g, f32x4& acc) {
     const Scales sc = scales(raw, g);
     f32x4 q = {0.f, 0.f, 0.f, 0.f};
@@ -259,6 +281,7 @@ struct Q4kRows {
 // NVFP4: lane g takes 64 weights, 32 nibble bytes and 4 scale bytes; e2m1 *
 // |scale| is exact in bf16.
 struct Nvfp4Rows {
+  static constexpr bool kDefinition = false;
   static constexpr int kUnit = 256;
   static constexpr bool kWholeUnits = false;
   struct X {
@@ -344,6 +367,7 @@ struct Nvfp4Rows {
 // L = 3 L mod 256, digit = 3 L / 256, on two bytes at a time; digit - 1 is
 // exact in fp16 and d is applied to the fp32 sums of the block.
 struct Tq1Rows {
+  static constexpr bool kDefinition = true;
   static constexpr int kUnit = 256;
   static constexpr bool kWholeUnits = true;
   struct X {
@@ -370,6 +394,22 @@ struct Tq1Rows {
                 ld16(make_rsrc(first, bytes), bytes - 2u)};
   }
   static __device__ __forceinline__ uint32_t row_offset(int k, int r) { return (uint32_t)r * (uint32_t)(k / 256 * 54); }
+  // one output by the definition, sum of (d * (digit - 1)) * x
+  static __device__ __forceinline__ float definition(const uint8_t* row, const uint16_t* x, int k) {
+    float sum = 0.f;
+    for (int b = 0; b < k / 256; ++b) {
+      const uint8_t* const blk = row + 54 * (int64_t)b;
+      const float d = (float)__builtin_bit_cast(_Float16, *reinterpret_cast<const unsigned short*>(blk + 52));
+      for (int e = 0; e < 256; ++e) {
+        const int at = e < 160 ? e % 32 : e < 240 ? 32 + e % 16 : 48 + e % 4;
+        const int dg = e < 160 ? e / 32 : e < 240 ? (e - 160) / 16 : (e - 240) / 4;
+        const unsigned l = (unsigned)blk[at] * pow3_u16(dg) & 255u;
+        const float v = (float)__builtin_bit_cast(_Float16, x[256 * b + e]);
+        sum = __builtin_fmaf(d * (float)((int)(3u * l >> 8) - 1), v, sum);
+      }
+    }
+    return sum;
+  }
   // fp16 codes of digit - 1 of the two bytes in the halves of l; l moves to the next digit
   static __device__ __forceinline__ unsigned digit(unsigned& l) {
     const unsigned p = __builtin_bit_cast(unsigned, __builtin_bit_cast(u16x2, l) * u16x2{3, 3});
@@ -458,6 +498,27 @@ struct Tq1Rows {
     for (int i = 0; i < 8; ++i) x.f[i] = *reinterpret_cast<const u32x4*>(xs + x_frag(i, g, col));
   }
 };
+
+// Q4_K and TQ1_0 apply a block's scales to its sum.  Where an activation or a scale is infinite
+// that is not what the definition gives: 0 * inf and inf - inf are NaN, and the
+// infinite scale of a zero weight is NaN only in the definition.  An output that is not finite
+// is therefore computed again by the definition, on one lane: one infinite activation
+// adds 180 us to a call with K = 4096 of Q4_K, 2 ms with 14336 of TQ1_0.
+
+__device__ __forceinline__ bool finite(float v) { return __builtin_fabsf(v) < __builtin_inff(); }
+
+// Stores output (tile row i, weight row `row`) again as F's definition gives it.
+template <typename F>
+__device__ __forceinline__ void store_definition(const RoutedArgs& a, const RoutedTile& t, int i, int row) {
+  int64_t at = t.first + i;
+  if (a.order) {
+    const int slot = a.order[at];
+    if ((unsigned)slot >= (unsigned)a.n) return;
+    at = slot / a.choices;
+  }
+  const float v = F::definition(a.w + t.e * a.expert_bytes + row * (a.expert_bytes / a.m), a.x + at * a.k, a.k);
+  store_y(a.y, a.y_dtype, (int64_t)(t.first + i) * a.m + row, v);
+}
 
 // A workgroup takes 16 RW weight rows, 16 a wave, times KW parts of K whose sums
 // meet in LDS at the end.  A wave copies its rows' packed bytes global -> LDS two
@@ -564,10 +625,15 @@ __global__ __launch_bounds__(64 * RW * KW, RW * KW == 4 ? 3 : 2) void routed_row
 #pragma unroll
     for (int p = 0; p < KW - 1; ++p) acc += sums[(p * RW + rw) * 64 + lane];
   }
+  unsigned again = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (4 * g + i < t.rows && n0 + col < a.m)
+    if (4 * g + i < t.rows && n0 + col < a.m) {
       store_y(a.y, a.y_dtype, (int64_t)(t.first + 4 * g + i) * a.m + n0 + col, acc[i]);
+      again |= finite(acc[i]) ? 0u : 1u << i;
+    }
+  if constexpr (F::kDefinition)
+    for (; again; again &= again - 1) store_definition<F>(a, t, 4 * g + __builtin_ctz(again), n0 + col);
 }
 
 // ---- many rows, Q4_K -----------------------------------------------------------------
@@ -713,6 +779,8 @@ __global__ __launch_bounds__(64 * kQ4kWaves, 2) void routed_q4k_kernel(RoutedArg
   else
     run(Int<TT / 2>{});
   wait_vm<0>();  // (no copy outlives the workgroup's LDS)
+  unsigned again = 0;  // bit 4 NR i + NR v + r: outputs to compute again
+  static_assert(4 * TT * NR <= 32, "a bit for each of a lane's outputs");
 #pragma unroll
   for (int i = 0; i < TT; ++i)
 #pragma unroll
@@ -722,9 +790,16 @@ __global__ __launch_bounds__(64 * kQ4kWaves, 2) void routed_q4k_kernel(RoutedArg
         const int64_t at = (int64_t)(t.first + tok) * a.m + n0 + col;
 #pragma unroll
         for (int r = 0; r < NR; ++r)
-          if (n0 + 16 * r + col < a.m) store_y(a.y, a.y_dtype, at + 16 * r, acc[i][r][v]);
+          if (n0 + 16 * r + col < a.m) {
+            store_y(a.y, a.y_dtype, at + 16 * r, acc[i][r][v]);
+            again |= finite(acc[i][r][v]) ? 0u : 1u << (4 * NR * i + NR * v + r);
+          }
       }
     }
+  for (; again; again &= again - 1) {
+    const int b = __builtin_ctz(again);
+    store_definition<F>(a, t, 16 * (b / (4 * NR)) + 4 * g + b / NR % 4, n0 + 16 * (b % NR) + col);
+  }
 }
 
 // ---- many rows --------------------------------------------------------------------

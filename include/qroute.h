@@ -95,7 +95,9 @@ int qroute_combine_grad(const void* dy, int32_t dy_dtype, const void* rows, int3
  *            has are left as they were.
  * Sums are in fp32, each output is rounded once to y_dtype, and weights are never
  * rounded: NVFP4's and TQ1_0's are exact in 16 bits, and Q4_K enters as
- * d * sum(scale * q * x) - dmin * sum(min * x) over each block.
+ * d * sum(scale * q * x) - dmin * sum(min * x) over each block.  Infinite and NaN
+ * activations and scales give what sum(weight * x) gives, in their own tokens' and rows'
+ * outputs alone.
  * K as for the prefill (K <= 2^20, NVFP4 K % 64 == 0), M <= 2^24, and with
  * `order` x spans at most 2^30 bytes.  T == 0 or M == 0 is a no-op. */
 int qgemm_q4k_routed(const void* w, const void* x_f16, const int32_t* order, const int32_t* offsets, void* y,

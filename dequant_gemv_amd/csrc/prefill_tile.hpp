@@ -1,8 +1,8 @@
 // The tile of a many-row product on packed weights: the formats' weight steps
 // (packed bytes to 16-bit MFMA inputs) and the K loop of one workgroup, whose
-// rows of activations and of outputs are described by an `Io` policy.  Used by
-// the prefill (prefill.hip, which describes the work split and the lane
-// layouts) and by the routed products (routed.hip).
+// caller copies the activations and stores the sums.  Used by the prefill
+// (prefill.hip, which describes the work split and the lane layouts) and by the
+// routed products (routed.hip).
 #pragma once
 #include "device.hpp"
 #include "launch.hpp"

@@ -10,7 +10,6 @@
 namespace qgemv {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned u32x3 __attribute__((ext_vector_type(3)));
 
 // x rows that are not there: beyond every x descriptor's range (at most 2^30
 // bytes), also when an offset of up to 2^31 is added.
@@ -83,17 +82,6 @@ __device__ __forceinline__ void store_y(void* y, int dtype, int64_t at, float v)
     static_cast<_Float16*>(y)[at] = (_Float16)pin_f32(v);
   else
     static_cast<__bf16*>(y)[at] = (__bf16)pin_f32(v);
-}
-
-// Four consecutive outputs (at a multiple of 4, y 16-byte aligned).
-__device__ __forceinline__ void store_y4(void* y, int dtype, int64_t at, f32x4 v) {
-  if (dtype == kF32) {
-    *reinterpret_cast<f32x4*>(static_cast<float*>(y) + at) = v;
-  } else {
-    const u32x2 p = dtype == kF16 ? u32x2{pf_pack2<_Float16>(v[0], v[1]), pf_pack2<_Float16>(v[2], v[3])}
-                                  : u32x2{pf_pack2<__bf16>(v[0], v[1]), pf_pack2<__bf16>(v[2], v[3])};
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(y) + at) = p;
-  }
 }
 
 }  // namespace qgemv

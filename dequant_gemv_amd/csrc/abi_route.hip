@@ -33,7 +33,7 @@ int gemm_routed(Fmt f, RouteFmt rf, const void* w, const void* x, const int32_t*
   if (e < 1 || e > QROUTE_MAX_E || m > kMaxK || kk > kPrefillMaxK) return QGEMV_E_SHAPE;
   if (f == kNvfp4 && kk % 64 != 0) return QGEMV_E_SHAPE;  // whole 64-weight steps
   const int64_t n = t * k;
-  if (n > 0 && m > 0 && routed_work_items(routed_plan(rf, n, e, m, kk)) > kMaxWorkItems) return QGEMV_E_SHAPE;
+  if (n > 0 && m > 0 && routed_work_items(routed_plan(rf, n, e, m)) > kMaxWorkItems) return QGEMV_E_SHAPE;
   if (order && t * kk * 2 > kRouteMaxXBytes) return QGEMV_E_SHAPE;
   if (!valid_dtype(y_dtype)) return QGEMV_E_DTYPE;
   if (t == 0 || m == 0) return QGEMV_OK;

@@ -65,8 +65,8 @@ struct RoutedPlan {
   int64_t tiles;   // of tokens, at most
 };
 
-// The launch of n > 0 slots over e weight sets of m > 0 rows and k columns.
-inline RoutedPlan routed_plan(int fmt, int64_t n, int64_t e, int64_t m, int64_t k) {
+// The launch of n > 0 slots over e weight sets of m > 0 rows.
+inline RoutedPlan routed_plan(int fmt, int64_t n, int64_t e, int64_t m) {
   const bool q4k = fmt == kRouteQ4k;
   const int64_t used = n < e ? n : e;
   const int64_t rows = n / used;  // of a weight set, on average
@@ -102,11 +102,12 @@ inline RoutedPlan routed_plan(int fmt, int64_t n, int64_t e, int64_t m, int64_t 
     // make at most one workgroup a CU (Q4_K, one token, two weight sets: 14336 x
     // 4096 15.3 / 19.1 / 28.6 us in this order, 8192 x 4096 12.0 / 10.8 / 15.5,
     // 4096 x 4096 11.6 / 11.1 / 9.3, 4096 x 14336 30.6 / 28.4 / 17.7).
-    // (TQ1_0, whose decoding takes longer than its few bytes, in two parts also for long
-    // rows: 74 slots over 8 weight sets of 4096 x 14336, at the time 60 us with two parts,
-    // 70 with one or with four, 64 with 128 rows and two parts)
+    // (TQ1_0, whose decoding takes longer than its few bytes, in two parts while the workgroups
+    // are at most two a CU: 74 slots over 8 weight sets, us with two parts and with one: 4096 x
+    // 2048 13.5, 13.2; x 4096 20.5, 20.8; x 8192 32.2, 34.9; x 14336 50.6, 53.7; 2560 x 8192 30.9,
+    // 33.6; 4608 x 8192 45.3, 43.7; 8192 x 4096 34.4, 30.0; 8192 x 14336 110.7, 107.5)
     p.rw = few <= 128 ? 2 : 4;
-    p.kw = few <= 128 ? 4 : few <= 256 || (fmt == kRouteTq1 && k > 8192) ? 2 : 1;
+    p.kw = few <= 128 ? 4 : few <= (fmt == kRouteTq1 ? 512 : 256) ? 2 : 1;
     p.threads = 64 * p.rw * p.kw;
     p.groups = (m + 16 * p.rw - 1) / (16 * p.rw);
     p.tiles = max_tiles(n, e, 16);

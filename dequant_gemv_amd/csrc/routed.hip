@@ -878,7 +878,7 @@ __global__ __launch_bounds__(64 * kPfWaves, BT == 64 ? 2 : 1) void routed_tile_k
 
 template <typename FR, typename FT>
 static hipError_t launch_routed(int fmt, RoutedArgs a, hipStream_t s) {
-  const RoutedPlan p = routed_plan(fmt, a.n, a.e_count, a.m, a.k);
+  const RoutedPlan p = routed_plan(fmt, a.n, a.e_count, a.m);
   a.groups = (int)p.groups;
   const dim3 grid((unsigned)(p.groups * p.tiles)), block((unsigned)p.threads);
   const auto rows = [&](auto rw, auto kw) {

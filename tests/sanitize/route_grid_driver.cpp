@@ -41,8 +41,8 @@ hipError_t launch_route_combine_grad(const void*, int, const void*, int, const i
   return items("combine_grad", route_grad_workgroups(t, c) * kRouteMoveThreads, t, k, c);
 }
 hipError_t launch_routed(int fmt, const void*, const void*, const int32_t*, const int32_t*, void*, int, int64_t t,
-                         int64_t choices, int64_t e, int64_t m, int64_t k, int64_t, hipStream_t) {
-  return items("product", routed_work_items(routed_plan(fmt, t * choices, e, m, k)), t * choices, m, e);
+                         int64_t choices, int64_t e, int64_t m, int64_t, int64_t, hipStream_t) {
+  return items("product", routed_work_items(routed_plan(fmt, t * choices, e, m)), t * choices, m, e);
 }
 int64_t lora_workspace(int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
 hipError_t launch_lora(bool, const void*, const void*, const void*, const float*, const int32_t*, const int32_t*,

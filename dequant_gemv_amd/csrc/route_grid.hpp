@@ -76,11 +76,15 @@ inline RoutedPlan routed_plan(int fmt, int64_t n, int64_t e, int64_t m) {
   };
   // What a kernel takes for 256 of K, in 1/100 us, by its workgroups: of 16 tokens
   // x 64 weight rows (K in parts while they are few, see below), 64 x 128 and 256 x 256
-  // (128 x 256 where weight sets have no more tokens).  Fitted to Q4_K through these three,
-  // 8 weight sets of 14336 x 4096 (us measured): 24 rows each 119, 126, -; 32
-  // rows 145, 129, -; 50 rows -, 154, 167; 64 rows -, 190, 171; 64 sets of 1024 x 4096, 32
-  // rows 88, 96, -.  Few weight rows leave large tiles a few CUs (TQ1_0, 102 rows of
-  // one set of 13 x 13568: 21, -, 267; 5 sets of 726 x 9216, 362 rows: 99, -, 269).
+  // (128 x 256 where weight sets have no more tokens).  Fitted to Q4_K through these three;
+  // at 31 sizes of each, NVFP4 and TQ1_0 come within 12% of the best of the three but for one
+  // (TQ1_0, 256 rows of each of two sets of 4096 x 14336: 228 us, 171 by the first).  Us by
+  // the three, NVFP4 / TQ1_0, 8 sets of 14336 x 4096: 34 rows each 135, 131, 151 / 122, 137,
+  // 161; 48 rows 171, 135, 153 / 152, 139, 161; 64 rows 217, 182, 159 / 191, 200, 185; 128
+  // rows 386, 293, 233 / 346, 298, 224.  Few weight rows leave large tiles a few CUs: one set
+  // of 512 x 13568, 400 rows: 29, 121, 313 / 32, 140, 386.  The average hides a popular
+  // set: 1024 tokens over 64 sets of 1024 x 4096, one with seven tenths of them, take 74 us
+  // against 46 for an even spread (Q4_K; NVFP4 56 and 54, TQ1_0 46 and 43).
   const int64_t few = tiles(16) * ((m + 63) / 64), mid = tiles(64) * ((m + 127) / 128);
   const int64_t big = tiles(256) * ((m + 255) / 256);
   const int64_t cost_few = few <= 128 ? 35 : few <= 256 ? 50 : 20 + 50 * few / 256;

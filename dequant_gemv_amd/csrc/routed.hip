@@ -529,8 +529,9 @@ __device__ __forceinline__ void store_definition(const RoutedArgs& a, const Rout
 //
 // Measured: Q4_K, one token through two sets of 14336 x 4096 in 16.8 us (66 MB, 3.9 TB/s,
 // a launch's start included); NVFP4, 64 tokens x 8 over 64 sets of 1024 x 4096 in 40.8
-// us (3.7 TB/s); TQ1_0, 74 slots over 8 sets of 4096 x 14336 in 47.5 us, where the
-// digits (VALU) and the operand reads (LDS) take about half each.
+// us (3.7 TB/s); TQ1_0, 74 slots over 8 sets of 4096 x 14336 in 50 to 57 us by box, of
+// which its VALU instructions (digits, mostly) are 31 by themselves and the rest operand
+// reads from LDS and barriers that nothing covers.
 constexpr int kStRing = 3;
 
 template <typename F, int RW, int KW>
@@ -648,11 +649,12 @@ __global__ __launch_bounds__(64 * RW * KW, RW * KW == 4 ? 3 : 2) void routed_row
 // into registers at the unit's end; the activations go from registers, loaded a unit
 // ahead, into operand order in the other of two LDS buffers.  One barrier a unit.
 //
-// Q4_K, 2048 tokens x 2 over 8 sets of 14336 x 4096: 725 us (0.66 PFLOP/s of the weights'
-// own products), bound by issue: 370 VALU instructions (decoding 200, activations and
-// their sums 75, scaling 64) and 72 MFMAs a unit and wave.  With weights rounded to fp16
-// in LDS and tiles of 256 x 256 the same took 615 us, but 64 to 512 rows of each of the
-// sets took 115 to 160 us, 82 to 140 like this.  Tiles of 96 tokens: 719 us, but 128 us
+// Q4_K, 2048 tokens x 2 over 8 sets of 14336 x 4096: 700 to 725 us (0.67 PFLOP/s of the
+// weights' own products; eight qgemm_q4k calls of 512 rows each, whose weights are
+// rounded, take 590 to 650), bound by issue: 370 VALU instructions (decoding 200,
+// activations and their sums 75, scaling 64) and 72 MFMAs a unit and wave.  With weights
+// rounded to fp16 in LDS and tiles of 256 x 256 the same took 615 us, but 24 to 64 rows of
+// each of the sets took 117 to 160 us, 83 to 139 like this.  Tiles of 96 tokens: 719 us, but 128 us
 // against 101 for 512 rows of one set; 48 weight rows a wave: 728, 133; 16 waves of 16
 // rows: 788, 104.
 __global__ __launch_bounds__(64 * kQ4kWaves, 2) void routed_q4k_kernel(RoutedArgs a) {
@@ -846,11 +848,11 @@ __device__ __forceinline__ void routed_tile(const RoutedArgs& a, const RoutedTil
 }
 
 // Tiles of 64 tokens x 128 weight rows, or of 256 x 256; a weight set's last tile
-// of 256 may have few tokens, and runs as one of 64 or 128 when it has no more
-// (Q4_K, 125 rows in each of 16 sets of 4096 x 4096: 182 us, 186 without the 64).  Bound as
-// the prefill is, by the matrix cores' operands through LDS: Q4_K, 2048 tokens x 2
-// over 8 sets of 14336 x 4096 in 590 to 650 us (0.8 PFLOP/s, matrix units busy a third
-// of the cycles at 2.4 GHz).
+// of 256 may have few tokens, and runs as one of 64 or 128 when it has no more (48 rows
+// in each of 32 sets of 4096 x 4096: NVFP4 165 us, 172 without the 64; TQ1_0 175, 188).
+// Bound as the prefill is, by the matrix cores' operands through LDS: 2048 tokens x 2
+// over 8 sets of 14336 x 4096 in 525 us (NVFP4, 0.92 PFLOP/s) and 615 us (TQ1_0, whose digits
+// take longer); eight qgemm_* calls of 512 rows each take 604 and 638.
 template <typename F, int BT, int NB>
 __global__ __launch_bounds__(64 * kPfWaves, BT == 64 ? 2 : 1) void routed_tile_kernel(RoutedArgs a) {
   typedef PfShape<BT, NB> S;

@@ -210,6 +210,7 @@ struct Q4kRows {
           const float v = (float)__builtin_bit_cast(_Float16, x[256 * b + 32 * g + i]);
           sum = __builtin_fmaf(__builtin_fmaf(ds, (float)q, -least), v, sum);
         }
+        if (sum != sum) return sum;  // (and stays NaN)
       }
     }
     return sum;
@@ -406,6 +407,7 @@ struct Tq1Rows {
         const unsigned l = (unsigned)blk[at] * pow3_u16(dg) & 255u;
         const float v = (float)__builtin_bit_cast(_Float16, x[256 * b + e]);
         sum = __builtin_fmaf(d * (float)((int)(3u * l >> 8) - 1), v, sum);
+        if (sum != sum) return sum;  // (and stays NaN)
       }
     }
     return sum;
@@ -502,8 +504,9 @@ struct Tq1Rows {
 // Q4_K and TQ1_0 apply a block's scales to its sum.  Where an activation or a scale is infinite
 // that is not what the definition gives: 0 * inf and inf - inf are NaN, and the
 // infinite scale of a zero weight is NaN only in the definition.  An output that is not finite
-// is therefore computed again by the definition, on one lane: one infinite activation
-// adds 180 us to a call with K = 4096 of Q4_K, 2 ms with 14336 of TQ1_0.
+// is therefore computed again by the definition, on one lane, up to where it is NaN: one infinite
+// activation adds 180 us to a call with K = 4096 of Q4_K, 3 ms with 14336 of TQ1_0; where
+// all activations are NaN, 2048 tokens x 2 of 14336 x 4096 take 2.5 ms.
 
 __device__ __forceinline__ bool finite(float v) { return __builtin_fabsf(v) < __builtin_inff(); }
 
